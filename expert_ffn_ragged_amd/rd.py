@@ -194,14 +194,22 @@ def _launch(fn, tensors, stream, *args):
             _check(fn(*args, handle))
 
 
-def _on_stream(stream, *tensors):
-    """Tie tensors allocated here (torch's current stream) to the stream the kernels run on, so the
-    caching allocator does not hand their memory out again before that stream is done with them."""
+def _empty(shape, dtype, device, stream):
+    """A new tensor for the kernels of a call on ``stream`` (None: torch's current one).
+
+    It comes from that stream's memory: the current stream's may still be in use by work that was queued there
+    before its tensor was freed, and nothing orders the call after that work.  The caller goes on with the tensor
+    on the current stream, so the caching allocator waits for that one too when it is freed.
+    """
     if stream is None:
-        return
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+        return torch.empty(shape, dtype=dtype, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream on {stream.device}, operands on {device}")
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
 
 
 def tile_count():
@@ -275,19 +283,15 @@ def ragged_dot(x, w, group_sizes, group_offset=None, limit=None, trans_rhs=False
         kw, n = w.shape[1], w.shape[2]
     if kw != k:
         raise ValueError("contraction sizes of x and w differ")
-    fresh = out is None
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=x.device)
+        out = _empty((m, n), out_dtype, x.device, stream)
     _need(out, "out", out.dtype, 2)
     if tuple(out.shape) != (m, n) or out.dtype not in _DTYPES:
         raise ValueError("out must be [m, n] bf16 or float32")
     lib = library()
     ws_bytes = lib.rd_forward_workspace_size(m, k, n, gl, 1 if trans_rhs else 0)
     if ws_bytes and (workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
-        _on_stream(stream, workspace)
-    if fresh:
-        _on_stream(stream, out)
+        workspace = _empty(ws_bytes, torch.uint8, x.device, stream)
     fn = lib.rd_forward_trans_rhs if trans_rhs else lib.rd_forward
     _launch(fn, (x, w, group_sizes, group_offset, limit, out, workspace if ws_bytes else None), stream,
             _ptr(x), _ptr(w), _ptr(group_sizes), group_sizes.numel(), _ptr(group_offset), gl, _ptr(limit), _ptr(out),
@@ -309,8 +313,7 @@ def ragged_dot_noalloc(x, w, group_sizes, group_offset=None, limit=None, out=Non
     if kw != k:
         raise ValueError("contraction sizes of x and w differ")
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
-        _on_stream(stream, out)
+        out = _empty((m, n), torch.bfloat16, x.device, stream)
     _need(out, "out", out.dtype, 2)
     if tuple(out.shape) != (m, n) or out.dtype not in _DTYPES:
         raise ValueError("out must be [m, n] bf16 or float32")
@@ -340,8 +343,7 @@ def ragged_dot_fp8(x, w, group_sizes, group_offset=None, limit=None, trans_rhs=F
     if kw != k:
         raise ValueError("contraction sizes of x and w differ")
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=x.device)
-        _on_stream(stream, out)
+        out = _empty((m, n), out_dtype, x.device, stream)
     _need(out, "out", out.dtype, 2)
     if tuple(out.shape) != (m, n) or out.dtype not in _DTYPES:
         raise ValueError("out must be [m, n] bf16 or float32")
@@ -370,8 +372,7 @@ def trans_ragged_dot_fp8(x, dy, group_sizes, num_local=None, group_offset=None, 
     n = dy.shape[1]
     gl = group_sizes.numel() if num_local is None else int(num_local)
     if out is None:
-        out = torch.empty((gl, k, n), dtype=out_dtype, device=x.device)
-        _on_stream(stream, out)
+        out = _empty((gl, k, n), out_dtype, x.device, stream)
     _need(out, "out", out.dtype, 3)
     if tuple(out.shape) != (gl, k, n) or out.dtype not in _DTYPES:
         raise ValueError("out must be [num_local, k, n] bf16 or float32")
@@ -383,8 +384,7 @@ def trans_ragged_dot_fp8(x, dy, group_sizes, num_local=None, group_offset=None, 
     elif row_split:
         ws_bytes = lib.rd_trans_workspace_size(m, k, n, gl)
         if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
-            _on_stream(stream, workspace)
+            workspace = _empty(ws_bytes, torch.uint8, x.device, stream)
     _launch(lib.rd_trans_fp8, (x, dy, group_sizes, group_offset, limit, out, workspace if ws_bytes else None), stream,
             _ptr(x), _ptr(dy), _ptr(group_sizes), group_sizes.numel(), _ptr(group_offset), gl, _ptr(limit),
             _ptr(out), _DTYPES[out.dtype], m, k, n, _ptr(workspace) if ws_bytes else None, ws_bytes)
@@ -415,14 +415,12 @@ def ragged_dot_glu(x, wi, group_sizes, group_offset=None, limit=None, act=None, 
         raise ValueError("wi must be [num_local, k, 2h] with x's k")
     h = h2 // 2
     if act is None:
-        act = torch.empty((m, h), dtype=torch.bfloat16, device=x.device)
-        _on_stream(stream, act)
+        act = _empty((m, h), torch.bfloat16, x.device, stream)
     _need(act, "act", torch.bfloat16, 2)
     if tuple(act.shape) != (m, h):
         raise ValueError("act must be [m, h]")
     if fused is None and want_fused:
-        fused = torch.empty((m, h2), dtype=torch.bfloat16, device=x.device)
-        _on_stream(stream, fused)
+        fused = _empty((m, h2), torch.bfloat16, x.device, stream)
     if fused is not None:
         _need(fused, "fused", torch.bfloat16, 2)
         if tuple(fused.shape) != (m, h2):
@@ -451,9 +449,8 @@ def trans_ragged_dot(x, dy, group_sizes, num_local=None, group_offset=None, limi
         raise ValueError("x and dy must have the same rows")
     n = dy.shape[1]
     gl = group_sizes.numel() if num_local is None else int(num_local)
-    fresh = out is None
     if out is None:
-        out = torch.empty((gl, k, n), dtype=out_dtype, device=x.device)
+        out = _empty((gl, k, n), out_dtype, x.device, stream)
     _need(out, "out", out.dtype, 3)
     if tuple(out.shape) != (gl, k, n) or out.dtype not in _DTYPES:
         raise ValueError("out must be [num_local, k, n] bf16 or float32")
@@ -465,10 +462,7 @@ def trans_ragged_dot(x, dy, group_sizes, num_local=None, group_offset=None, limi
     elif row_split:
         ws_bytes = lib.rd_trans_workspace_size(m, k, n, gl)
         if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
-            _on_stream(stream, workspace)
-    if fresh:
-        _on_stream(stream, out)
+            workspace = _empty(ws_bytes, torch.uint8, x.device, stream)
     _launch(lib.rd_trans, (x, dy, group_sizes, group_offset, limit, out, workspace if ws_bytes else None), stream,
             _ptr(x), _ptr(dy), _ptr(group_sizes), group_sizes.numel(), _ptr(group_offset), gl, _ptr(limit),
             _ptr(out), _DTYPES[out.dtype], m, k, n, _ptr(workspace) if ws_bytes else None, ws_bytes)
@@ -489,8 +483,7 @@ def glu_fwd(fused, limit=None, out=None, stream=None):
         raise ValueError("fused width must be even")
     h = two_h // 2
     if out is None:
-        out = torch.empty((rows, h), dtype=torch.bfloat16, device=fused.device)
-        _on_stream(stream, out)
+        out = _empty((rows, h), torch.bfloat16, fused.device, stream)
     _need(out, "out", torch.bfloat16, 2)
     if tuple(out.shape) != (rows, h):
         raise ValueError("out must be [rows, h]")
@@ -509,8 +502,7 @@ def glu_bwd(fused, d_out, limit=None, out=None, stream=None):
     if tuple(d_out.shape) != (rows, h):
         raise ValueError("d_out must be [rows, h]")
     if out is None:
-        out = torch.empty((rows, two_h), dtype=torch.bfloat16, device=fused.device)
-        _on_stream(stream, out)
+        out = _empty((rows, two_h), torch.bfloat16, fused.device, stream)
     _need(out, "out", torch.bfloat16, 2)
     if tuple(out.shape) != (rows, two_h):
         raise ValueError("out must be [rows, 2h]")
@@ -533,11 +525,9 @@ def unsort_bwd_rows(g, y, w, limit=None, grad=None, dot=None, stream=None):
     if tuple(y.shape) != (rows, hidden) or w.shape[0] != rows:
         raise ValueError("g and y must be [rows, hidden] and w [rows]")
     if grad is None:
-        grad = torch.empty((rows, hidden), dtype=torch.bfloat16, device=g.device)
-        _on_stream(stream, grad)
+        grad = _empty((rows, hidden), torch.bfloat16, g.device, stream)
     if dot is None:
-        dot = torch.empty((rows,), dtype=torch.float32, device=g.device)
-        _on_stream(stream, dot)
+        dot = _empty((rows,), torch.float32, g.device, stream)
     _need(grad, "grad", torch.bfloat16, 2)
     _need(dot, "dot", torch.float32, 1)
     if tuple(grad.shape) != (rows, hidden) or dot.shape[0] != rows:
