@@ -35,12 +35,13 @@ struct RowsArgs {
   int chunks;            // 16-byte chunks per row
   long long rows;        // rows of the sorted buffer
   int parts;             // parts a row is cut into (one wave each)
+  int first;             // the launch's first wave
 };
 
-// The wave's number in the grid, known to be the same in its lanes (slots and weights then come through
+// The wave's number in the call, known to be the same in its lanes (slots and weights then come through
 // the scalar cache, and their addresses stay out of the vector registers).
-__device__ __forceinline__ long long wave_index() {
-  return __builtin_amdgcn_readfirstlane(static_cast<int>(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)));
+__device__ __forceinline__ long long wave_index(const RowsArgs& p) {
+  return __builtin_amdgcn_readfirstlane(p.first + static_cast<int>(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)));
 }
 __device__ __forceinline__ long long slot_of(const RowsArgs& p, long long t, int i) {
   const long long s = p.slots[t * p.K + i];
@@ -55,7 +56,7 @@ constexpr int kChunks = 8;  // 16-byte chunks of a row that a lane of dispatch c
 // rows that were gathered 289, and 4 KB a wave 227.  (1 KB a wave gains 0.2 us below 128 choices and loses from 512.)
 __global__ __launch_bounds__(kThreads) void dispatch_rows_kernel(RowsArgs p) {
   const int lane = threadIdx.x & 63;
-  const long long unit = wave_index();
+  const long long unit = wave_index(p);
   const long long choice = unit / p.parts;
   if (choice >= static_cast<long long>(p.T) * p.K) return;
   const int part = static_cast<int>(unit - choice * p.parts);
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_rows_kernel(RowsArgs p) {
 __global__ __launch_bounds__(kThreads) void combine_rows_kernel(RowsArgs p) {
   constexpr int AT = 4;
   const int lane = threadIdx.x & 63;
-  const long long unit = wave_index();
+  const long long unit = wave_index(p);
   const long long t = unit / p.parts;
   if (t >= p.T) return;
   const int part = static_cast<int>(unit - t * p.parts);
@@ -118,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(RowsArgs p) {
 // 0.60 GB (g's rows come from the caches after the first choice), 112 us (5.4 TB/s).
 __global__ __launch_bounds__(kThreads) void combine_rows_bwd_kernel(RowsArgs p) {
   const int lane = threadIdx.x & 63;
-  const long long unit = wave_index();
+  const long long unit = wave_index(p);
   const long long t = unit / p.K;
   if (t >= p.T) return;
   const long long s = slot_of(p, t, static_cast<int>(unit - t * p.K));
@@ -143,9 +144,17 @@ __global__ __launch_bounds__(kThreads) void combine_rows_bwd_kernel(RowsArgs p) 
   if (lane == 0) p.dw[unit] = static_cast<float>(acc);
 }
 
-int blocks_of(long long units) {
-  const long long b = (units + kThreads / 64 - 1) / (kThreads / 64);
-  return static_cast<int>(b < 1 ? 1 : b);
+// One wave a unit, in launches of 2^25: a launch takes fewer than 2^32 threads.  units < 2^31.
+template <class Kernel>
+int launch_waves(Kernel kernel, RowsArgs a, long long units, hipStream_t stream) {
+  constexpr long long most = 1ll << 25, per = kThreads / 64;
+  for (long long first = 0; first < units; first += most) {
+    a.first = static_cast<int>(first);
+    const long long n = units - first < most ? units - first : most;
+    kernel<<<static_cast<int>((n + per - 1) / per), kThreads, 0, stream>>>(a);
+    if (hipGetLastError() != hipSuccess) return RD_EHIP;
+  }
+  return RD_OK;
 }
 
 // per: chunks of a row that one wave carries
@@ -172,20 +181,17 @@ int launch_dispatch_rows(const RowsProblem& q, hipStream_t stream) {
   RowsArgs a = args_of(q, 64 * kChunks);
   const long long most = ((1ll << 31) - 8) / (choices > 0 ? choices : 1);  // waves are numbered in 32 bits
   if (a.parts > most) a.parts = static_cast<int>(most);  // >= 1: choices < 2^31, and a wave takes parts in turn
-  dispatch_rows_kernel<<<blocks_of(choices * a.parts), kThreads, 0, stream>>>(a);
-  return hipGetLastError() == hipSuccess ? RD_OK : RD_EHIP;
+  return launch_waves(dispatch_rows_kernel, a, choices * a.parts, stream);
 }
 
 int launch_combine_rows(const RowsProblem& q, hipStream_t stream) {
   const RowsArgs a = args_of(q, 64);
-  combine_rows_kernel<<<blocks_of(static_cast<long long>(a.T) * a.parts), kThreads, 0, stream>>>(a);
-  return hipGetLastError() == hipSuccess ? RD_OK : RD_EHIP;
+  return launch_waves(combine_rows_kernel, a, static_cast<long long>(a.T) * a.parts, stream);
 }
 
 int launch_combine_rows_bwd(const RowsProblem& q, hipStream_t stream) {
   const RowsArgs a = args_of(q, 64);
-  combine_rows_bwd_kernel<<<blocks_of(static_cast<long long>(a.T) * a.K), kThreads, 0, stream>>>(a);
-  return hipGetLastError() == hipSuccess ? RD_OK : RD_EHIP;
+  return launch_waves(combine_rows_bwd_kernel, a, static_cast<long long>(a.T) * a.K, stream);
 }
 
 }  // namespace rd

@@ -36,6 +36,7 @@ struct RouteArgs {
   int T, E, K, groups, top_groups;
   bool sigmoid, renorm;
   float scale;
+  int first;  // the launch's first row
 };
 
 // ---------------------------------------------------------------- a row's lanes
@@ -298,7 +299,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs p) {
   __shared__ double s_keys[GROUPS ? NW * RPW : 1][GROUPS ? EPL * LPR : 1];
   const int lane = threadIdx.x & 63, sub = lane & (LPR - 1), wave = threadIdx.x >> 6;
   const int slot = wave * RPW + lane / LPR;
-  const int row = blockIdx.x * (NW * RPW) + slot;
+  const int row = p.first + blockIdx.x * (NW * RPW) + slot;
   int L = p.T;
   if (p.limp != nullptr) {
     const int v = *p.limp;
@@ -370,6 +371,7 @@ struct RouteBwdArgs {
   int T, E, K;
   bool sigmoid, renorm;
   float scale;
+  int first;  // the launch's first row
 };
 
 // d_logits of one row.  With q the chosen scores: softmax without renormalisation
@@ -381,7 +383,7 @@ template <int EPL, int LPR, bool BF16>
 __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs p) {
   constexpr int RPW = 64 / LPR, NW = kThreads / 64;
   const int lane = threadIdx.x & 63, sub = lane & (LPR - 1), wave = threadIdx.x >> 6;
-  const int row = blockIdx.x * (NW * RPW) + wave * RPW + lane / LPR;
+  const int row = p.first + blockIdx.x * (NW * RPW) + wave * RPW + lane / LPR;
   const bool in = row < p.T;
   const long long base = static_cast<long long>(in ? row : 0) * p.E;
   int id = -1;
@@ -627,14 +629,23 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
   }
 }
 
+// LPR lanes a row, in launches of 2^23 workgroups: a launch takes fewer than 2^32 threads.
+template <int LPR, class Kernel, class Args>
+void launch_rows(Kernel kernel, Args a, hipStream_t stream) {
+  constexpr int per = kThreads / LPR, blocks = 1 << 23;
+  for (long long first = 0; first < a.T; first += static_cast<long long>(per) * blocks) {
+    a.first = static_cast<int>(first);
+    const long long want = (a.T - first + per - 1) / per;
+    kernel<<<static_cast<int>(want < blocks ? want : blocks), kThreads, 0, stream>>>(a);
+  }
+}
+
 template <int EPL, int LPR, int HEADS, bool BF16>
 void launch_route_as(const RouteArgs& a, hipStream_t stream) {
-  constexpr int rows = kThreads / LPR;
-  const int grid = (a.T + rows - 1) / rows;
   if (a.groups > 1)
-    route_kernel<EPL, LPR, HEADS, BF16, true><<<grid, kThreads, 0, stream>>>(a);
+    launch_rows<LPR>(route_kernel<EPL, LPR, HEADS, BF16, true>, a, stream);
   else
-    route_kernel<EPL, LPR, HEADS, BF16, false><<<grid, kThreads, 0, stream>>>(a);
+    launch_rows<LPR>(route_kernel<EPL, LPR, HEADS, BF16, false>, a, stream);
 }
 template <int EPL, int LPR, int HEADS>
 void launch_route_as(const RouteArgs& a, bool bf16, hipStream_t stream) {
@@ -646,12 +657,10 @@ void launch_route_as(const RouteArgs& a, bool bf16, hipStream_t stream) {
 
 template <int EPL, int LPR>
 void launch_route_bwd_as(const RouteBwdArgs& a, bool bf16, hipStream_t stream) {
-  constexpr int rows = kThreads / LPR;
-  const int grid = (a.T + rows - 1) / rows;
   if (bf16)
-    route_bwd_kernel<EPL, LPR, true><<<grid, kThreads, 0, stream>>>(a);
+    launch_rows<LPR>(route_bwd_kernel<EPL, LPR, true>, a, stream);
   else
-    route_bwd_kernel<EPL, LPR, false><<<grid, kThreads, 0, stream>>>(a);
+    launch_rows<LPR>(route_bwd_kernel<EPL, LPR, false>, a, stream);
 }
 
 int sort_blocks(long long n) {
@@ -674,7 +683,7 @@ void launch_sort(const int32_t* ids, int n, int experts, int blocks, int32_t* si
 
 int launch_route(const RouteProblem& q, hipStream_t stream) {
   RouteArgs a{q.logits, q.bias, q.limit, q.weights, q.ids, q.tokens, q.experts, q.top_k, q.groups, q.top_groups,
-              q.sigmoid, q.renorm, q.scale};
+              q.sigmoid, q.renorm, q.scale, 0};
   if (q.experts <= 64)
     launch_route_as<4, 16, 4>(a, q.bf16, stream);
   else if (q.experts <= 128)
@@ -689,7 +698,7 @@ int launch_route(const RouteProblem& q, hipStream_t stream) {
 }
 
 int launch_route_bwd(const RouteProblem& q, const float* d_weights, void* d_logits, hipStream_t stream) {
-  RouteBwdArgs a{q.logits, q.ids, d_weights, d_logits, q.tokens, q.experts, q.top_k, q.sigmoid, q.renorm, q.scale};
+  RouteBwdArgs a{q.logits, q.ids, d_weights, d_logits, q.tokens, q.experts, q.top_k, q.sigmoid, q.renorm, q.scale, 0};
   if (q.experts <= 64)
     launch_route_bwd_as<4, 16>(a, q.bf16, stream);
   else if (q.experts <= 128)

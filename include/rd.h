@@ -385,7 +385,7 @@ int rd_zero_rows_from_limit(void* buf, const int32_t* limit, int64_t rows, int64
  * Requirements: 1 <= experts <= RD_MAX_GROUPS; 1 <= top_k <= RD_MAX_TOP_K;
  * 1 <= top_groups <= groups <= RD_MAX_ROUTE_GROUPS; experts a multiple of
  * groups; top_k <= top_groups * (experts / groups); logits aligned to its
- * element; tokens < 2^31.  Nothing is launched when tokens is 0.
+ * element; tokens < 2^31 - 64.  Nothing is launched when tokens is 0.
  */
 int rd_route(const void* logits, int32_t dtype, const float* bias, const int32_t* limit, float* weights, int32_t* ids,
              int64_t tokens, int32_t experts, int32_t top_k, int32_t score, int32_t groups, int32_t top_groups,
