@@ -107,6 +107,15 @@ __device__ __forceinline__ Window build_local_bounds(const int32_t* __restrict__
   return Window{s_lb[0], s_lb[gl], L};
 }
 
+// ceil(rows / tile) for rows (or columns) in [0, 2^31): rows + tile - 1 may pass 2^31.
+__host__ __device__ constexpr int row_blocks(int rows, int tile) {
+  return static_cast<int>((static_cast<uint32_t>(rows) + static_cast<uint32_t>(tile) - 1u) / static_cast<uint32_t>(tile));
+}
+static_assert(row_blocks(0, 128) == 0 && row_blocks(1, 128) == 1 && row_blocks(128, 128) == 1 &&
+                  row_blocks(129, 128) == 2 && row_blocks(0x7FFFFFFF, 128) == 1 << 24 &&
+                  row_blocks(0x7FFFFFFF - 127, 256) == 1 << 23 && row_blocks(0x7FFFFFFF, 16) == 1 << 27,
+              "rounds up for every row count");
+
 // s_out[j] = sum_{i<j} cnt(i) for j in [0, n], cnt(i) = ceil((s_lb[i+1]-s_lb[i]) / tile).
 // Returns the total.  Requires n <= 4 * NT.  Ends with a barrier.
 template <int NT = kThreads>
@@ -117,7 +126,7 @@ __device__ __forceinline__ int tile_prefix(const int* s_lb, int n, int tile, int
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int j = 4 * t + i;
-    c[i] = j < n ? (s_lb[j + 1] - s_lb[j] + tile - 1) / tile : 0;
+    c[i] = j < n ? row_blocks(s_lb[j + 1] - s_lb[j], tile) : 0;
     tot += c[i];
   }
   long long run = block_excl_scan<NT>(tot, s_wave);

@@ -535,19 +535,18 @@ __global__ __launch_bounds__(kTileThreads, kTileWgs<MAXL>) void ragged_dot_mx_ti
   __shared__ int s_tiles[MAXL + 1];  // this XCD's tiles before each group
   __shared__ long long s_wave[kTileWaves];
   const Window win = build_local_bounds<kTileThreads>(p.gs, p.G, p.offp, p.gl, p.limp, p.m, s_lb, s_wave);
-  const int strips = (p.n + kTileN - 1) / kTileN;
+  const int strips = row_blocks(p.n, kTileN);
   const int xcd = blockIdx.x % kXcds, step = gridDim.x / kXcds;  // the grid is a multiple of kXcds
   // strips of group j on this XCD: s with (j * strips + s) % kXcds == xcd
   const auto first_strip = [&](int j) { return static_cast<int>((xcd + kXcds - (static_cast<long long>(j) * strips) % kXcds) % kXcds); };
   const auto strips_here = [&](int j) { return (strips - first_strip(j) + kXcds - 1) / kXcds; };
-  const auto row_blocks = [&](int j) { return (s_lb[j + 1] - s_lb[j] + kTileM - 1) / kTileM; };
   {
     constexpr int PER = (MAXL + kTileThreads) / kTileThreads;
     int c[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int j = PER * threadIdx.x + i;
-      c[i] = j < p.gl ? row_blocks(j) * strips_here(j) : 0;
+      c[i] = j < p.gl ? row_blocks(s_lb[j + 1] - s_lb[j], kTileM) * strips_here(j) : 0;
       sum += c[i];
     }
     int run = static_cast<int>(block_excl_scan<kTileThreads>(sum, s_wave));
@@ -564,7 +563,7 @@ __global__ __launch_bounds__(kTileThreads, kTileWgs<MAXL>) void ragged_dot_mx_ti
     TileAt t;
     t.j = __builtin_amdgcn_readfirstlane(upper_index(s_tiles, p.gl, tile));
     const int lb = __builtin_amdgcn_readfirstlane(s_lb[t.j]), ub = __builtin_amdgcn_readfirstlane(s_lb[t.j + 1]);
-    const int mts = (ub - lb + kTileM - 1) / kTileM;
+    const int mts = row_blocks(ub - lb, kTileM);
     const int local = tile - __builtin_amdgcn_readfirstlane(s_tiles[t.j]);
     const int unit = local / mts;
     t.once = mts == 1;
@@ -597,14 +596,14 @@ __global__ __launch_bounds__(kTileThreads, kTileWgs<MAXL>) void ragged_dot_mx_ti
 template <int XB>
 void launch_mx(const MxArgs& a, hipStream_t stream) {
   const long long cus = device_cu_count();
-  const long long strips = (a.n + kTileN - 1) / kTileN;
+  const long long strips = row_blocks(a.n, kTileN);
   if (a.m <= static_cast<long long>(kFewRows) * a.gl && a.gl * strips <= kFewTiles) {
-    const long long passes = (((a.m + 15) / 16 + a.gl) * ((a.n + 15) / 16) + kFewN - 1) / kFewN;
+    const long long passes = ((row_blocks(a.m, 16) + a.gl) * ((a.n + 15ll) / 16) + kFewN - 1) / kFewN;
     const int grid = static_cast<int>(passes < cus * 2 ? passes : cus * 2);
     ragged_dot_mx_few<XB><<<grid, kThreads, 0, stream>>>(a);
     return;
   }
-  const long long tiles = ((a.m + kTileM - 1) / kTileM + a.gl) * strips;
+  const long long tiles = (row_blocks(a.m, kTileM) + a.gl) * strips;
   const auto grid = [&](long long wgs) {
     const long long most = cus * wgs / kXcds * kXcds, want = tiles < most ? (tiles + kXcds - 1) / kXcds * kXcds : most;
     return static_cast<int>(want > 0 ? want : kXcds);
