@@ -94,11 +94,19 @@ struct Exp2Terms {  // (ln 2)^k / k!
   }
 };
 
-// 2^t for t in [-1100, 1022], NaN for NaN: the power series at the distance to the nearest whole number,
-// whose term k = 14 is below 2^-57.
-__device__ __forceinline__ double exp2_of(double t) {
+// x log2(e) as a whole number n and the rest r, |r| <= 1: log2(e) in two parts (the second is log2(e) less its
+// double), so that r is off by 2^-53 however large x is, where x log2(e) rounded once would be off by |x| 2^-53.
+struct Power {
+  double n, r;
+};
+__device__ __forceinline__ Power power_of(double x) {
+  constexpr double hi = 1.4426950408889634, lo = 2.0355273740931033e-17;
+  const double n = __builtin_rint(x * hi);
+  return {n, __builtin_fma(x, lo, __builtin_fma(x, hi, -n))};
+}
+// 2^(n + r) for n in [-1100, 1022], |r| <= 1/2, NaN for NaN: the power series, whose term k = 14 is below 2^-57.
+__device__ __forceinline__ double exp2_of(double n, double r) {
   constexpr Exp2Terms T;
-  const double n = __builtin_rint(t), r = t - n;
   double v = T.c[13];
 #pragma unroll
   for (int k = 12; k >= 0; --k) v = __builtin_fma(v, r, T.c[k]);
@@ -106,9 +114,17 @@ __device__ __forceinline__ double exp2_of(double t) {
 }
 // e^x, the argument cut to where the result and 1 / (1 + result) are normal numbers
 __device__ __forceinline__ double exp_of(double x) {
-  double t = x * 1.4426950408889634074;
-  t = t > 1022.0 ? 1022.0 : t;
-  return exp2_of(t < -1100.0 ? -1100.0 : t);
+  x = x > 708.0 ? 708.0 : x;
+  const Power p = power_of(x < -762.0 ? -762.0 : x);
+  return exp2_of(p.n, p.r);
+}
+// e^(x - m), m the power of the largest x: the difference is taken after the multiplication, since x - m itself
+// may need more than 53 bits
+__device__ __forceinline__ double exp_below(double x, double largest, const Power& m) {
+  const Power p = power_of(x);
+  const double r = p.r - m.r, k = __builtin_rint(r);
+  const double v = exp2_of(p.n - m.n + k, r - k);
+  return x - largest < -762.0 ? 0.0 : v;
 }
 // 1 / y for a normal y: the hardware's estimate and two Newton steps
 __device__ __forceinline__ double inverse(double y) {
@@ -127,9 +143,11 @@ __device__ __forceinline__ bool scores(const float (&x)[EPL], float row_max, boo
     return false;
   }
   double sum = 0.0;
+  const double largest = row_max;
+  const Power m = power_of(largest);
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    s[j] = j * LPR + sub < E ? exp_of(static_cast<double>(x[j]) - static_cast<double>(row_max)) : 0.0;
+    s[j] = j * LPR + sub < E ? exp_below(static_cast<double>(x[j]), largest, m) : 0.0;
     sum += s[j];
   }
   sum = row_all<LPR>(sum, Add<double>());

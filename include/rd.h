@@ -376,8 +376,10 @@ int rd_zero_rows_from_limit(void* buf, const int32_t* limit, int64_t rows, int64
  * s_e (+ bias_e) of its unmasked experts, and only experts of the top_groups
  * best groups take part.  The top_k largest keys are chosen in descending
  * order, ties going to the lower index; the choice is that of exact
- * arithmetic on the given numbers as far as float64 tells them apart (2^-48 of
- * a key).  NaN ranks with +inf as the largest value.  A choice that no unmasked expert is left for has id
+ * arithmetic on the given numbers as far as float64 tells them apart: a score
+ * is off by at most 2^-47 of itself (scores below 2^-1022 keep fewer bits),
+ * whatever the size of the logits, and keys that differ in the last four bits of
+ * their float64 significands alone count as ties.  NaN ranks with +inf as the largest value.  A choice that no unmasked expert is left for has id
  * -1 and weight 0, and so have all choices of the rows at or past the limit.
  * weight = s of the chosen, divided by the row's sum of them where
  * renormalize is nonzero, times scale; float32.

@@ -266,3 +266,32 @@ def test_group_rows_of_many_workgroups(n, experts):
     place = torch.empty_like(want)
     place[want] = torch.arange(n, device=DEV)
     assert torch.equal(slots.long(), torch.where(inside, place, -1))
+
+
+
+# the float32 bits of four logits near -60, -300 and -650: e^x of the first two add up to less than of the last two,
+# by 2^-46.8, 2^-46.2 and 2^-45.4 of the sum (found by a search); the same number of steps added to each keeps that
+NEARLY_EQUAL = [(3261884010, 3261746672, 3261898511, 3261738448), (3281412638, 3281401802, 3281441263, 3281390346),
+                (3290613656, 3290584961, 3290610543, 3290585567)]
+
+
+@pytest.mark.parametrize("bits", NEARLY_EQUAL)
+def test_nearly_equal_groups_of_small_scores(bits):
+    """Two groups of two experts with nearly the same sum of scores, far below a third group's: the choice is that of
+    the exact sums.  The interface allows 2^-47 of a score; here sums are off by 2^-50, six roundings of half a step
+    each (exponential, reciprocal, sum)."""
+    n = 400
+    say(f"route nearly equal groups {bits}")
+    x = (np.array(bits, np.uint32) + np.arange(n, dtype=np.uint32)[:, None]).view(np.float32)
+    e = np.exp(x.astype(np.longdouble))  # sigmoid = e / (1 + e) and softmax = e / sum keep the order of sums of e
+    low, high = e[:, 0] + e[:, 1], e[:, 2] + e[:, 3]
+    assert np.all(high - low >= 2.0 ** -47 * high) and np.all(high - low <= 2.0 ** -45 * high)
+    rows = np.zeros((2 * n, 6), np.float32)
+    rows[:n, 2:], rows[n:, 2:] = x, x[:, [2, 3, 0, 1]]
+    want = np.repeat([2, 1], n)
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, torch.zeros(6, device=DEV)):
+            _, ids = rd.route(torch.from_numpy(rows).to(DEV), 4, bias=bias, score=score, groups=3, top_groups=2)
+            ids = ids.cpu().numpy()
+            assert np.array_equal(ids[:, :2], np.tile([0, 1], (2 * n, 1)))
+            assert np.array_equal(ids[:, 2] // 2, want) and np.array_equal(ids[:, 3] // 2, want), (score, bias is None)
