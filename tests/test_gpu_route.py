@@ -295,3 +295,20 @@ def test_nearly_equal_groups_of_small_scores(bits):
             ids = ids.cpu().numpy()
             assert np.array_equal(ids[:, :2], np.tile([0, 1], (2 * n, 1)))
             assert np.array_equal(ids[:, 2] // 2, want) and np.array_equal(ids[:, 3] // 2, want), (score, bias is None)
+
+
+@pytest.mark.parametrize("n", [511, 513, 1535, 1536, 1537, 2047, 2048, 2049, 4095])
+def test_group_rows_around_the_ids_a_lane_carries(n):
+    """One workgroup sorts 512, 1536, 2048 or 4096 ids with 1, 3, 4 or 8 a lane; against a stable sort."""
+    for experts in (1, 60, 1024):
+        say(f"group_rows {n} {experts}")
+        ids = np.random.default_rng(n + experts).integers(-1, experts + 1, size=n).astype(np.int32)
+        sizes, rows, slots, total = rd.group_rows(torch.from_numpy(ids).to(DEV), experts)
+        cls = np.where((ids < 0) | (ids >= experts), experts, ids)
+        want = np.argsort(cls, kind="stable")
+        place = np.empty(n, dtype=np.int64)
+        place[want] = np.arange(n)
+        assert np.array_equal(rows.cpu().numpy(), want)
+        assert np.array_equal(slots.cpu().numpy(), np.where(cls < experts, place, -1))
+        assert np.array_equal(sizes.cpu().numpy(), np.bincount(cls, minlength=experts + 1)[:experts])
+        assert int(total) == int((cls < experts).sum())
