@@ -49,7 +49,7 @@ OP_OF_KERNEL = (
     (r"trans_split_reduce", "trans_split_reduce"),
     (r"\broute_kernel", "route"),
     (r"route_bwd_kernel", "route_bwd"),
-    (r"sort_(count|place)_kernel", "group_rows"),
+    (r"sort_(count|scan|place)_kernel", "group_rows"),
     (r"dispatch_rows_kernel", "dispatch_rows"),
     (r"combine_rows_kernel", "combine_rows"),
     (r"combine_rows_bwd_kernel", "combine_rows_bwd"),

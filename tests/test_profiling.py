@@ -134,3 +134,17 @@ def test_api_region_flags_a_sync_and_a_host_copy(tmp_path):
     text = profiling.apitrace_summary(str(d), "cmd")
     assert "blocking copies among the calls: **1**" in text
     assert "Memory copies to or from the host: **1**" in text
+
+
+def test_every_kernel_of_the_library_has_an_op():
+    import glob
+    import re
+
+    found = set()
+    for path in glob.glob(os.path.join(profiling.HERE, "csrc", "*.hip")):
+        with open(path) as fh:
+            found |= set(re.findall(r"__global__\s+__launch_bounds__\((?:[^()]|\([^()]*\))*\)\s*void\s+(\w+)\(", fh.read()))
+    assert {"sort_count_kernel", "sort_scan_kernel", "sort_place_kernel", "ragged_dot_mx_tile", "route_kernel"} <= found
+    for name in sorted(found):
+        # the grouped GEMMs are told apart by their first template argument
+        assert profiling.op_of(name) or profiling.op_of(name + "<0, 128>"), name
