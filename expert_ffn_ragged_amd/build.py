@@ -42,6 +42,7 @@ SOURCES = [
     ("rd_gemm_mx.hip", []),
     ("rd_api.cpp", ["-x", "hip"]),
 ]
+MODULE_SOURCE = "rd_torch.cpp"
 
 
 def _run(cmd):
@@ -66,25 +67,44 @@ def _torch_flags():
     return include, ["-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
 
 
+def _obj(src):
+    return os.path.join(BUILD_DIR, src + ".o")
+
+
+def _compile_module():
+    """The host module's object; returns the flags to link it with, or None where torch is not installed."""
+    try:
+        include, libs = _torch_flags()
+    except ImportError as e:
+        sys.stderr.write(f"{e}: _rd.so (the routed layer's calls from PyTorch) is not built\n")
+        return None
+    _run([CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-I", INCLUDE, *include, "-c",
+          os.path.join(CSRC, MODULE_SOURCE), "-o", _obj(MODULE_SOURCE)])
+    return libs
+
+
 def build(verbose=False):
-    """Compile every source for gfx950 and link librd.so and _rd.so next to this file."""
+    """Compile every source for gfx950 and link librd.so and _rd.so next to this file.
+
+    librd.so needs hipcc alone and is there before a failure of the host module, which needs torch, a C++ compiler
+    and Python's headers, is raised.
+    """
     os.makedirs(BUILD_DIR, exist_ok=True)
-    include, libs = _torch_flags()
-    obj = lambda src: os.path.join(BUILD_DIR, src + ".o")  # noqa: E731
-    steps = [[HIPCC, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj(src)] for src, extra in SOURCES]
-    host = "rd_torch.cpp"
-    steps.append([CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-I", INCLUDE, *include, "-c",
-                  os.path.join(CSRC, host), "-o", obj(host)])
+    steps = [[HIPCC, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", _obj(src)] for src, extra in SOURCES]
+    # each is linked beside its place and moved there whole; _rd.so finds librd.so in its own folder
     with concurrent.futures.ThreadPoolExecutor(4) as pool:
-        for out in pool.map(_run, steps):
+        outs = pool.map(_run, steps)
+        module = pool.submit(_compile_module)
+        for out in outs:
             if verbose and out.strip():
                 print(out)
-    # each is linked beside its place and moved there whole; _rd.so finds librd.so in its own folder
-    _run([HIPCC, "-shared", f"--offload-arch={ARCH}", "-fPIC", "-Wl,-soname,librd.so",
-          *(obj(src) for src, _ in SOURCES), "-o", LIB + ".tmp"])
-    os.replace(LIB + ".tmp", LIB)
-    _run([CXX, "-shared", obj(host), LIB, *libs, "-Wl,-rpath,$ORIGIN", "-o", MODULE + ".tmp"])
-    os.replace(MODULE + ".tmp", MODULE)
+        _run([HIPCC, "-shared", f"--offload-arch={ARCH}", "-fPIC", "-Wl,-soname,librd.so",
+              *(_obj(src) for src, _ in SOURCES), "-o", LIB + ".tmp"])
+        os.replace(LIB + ".tmp", LIB)
+        libs = module.result()
+    if libs is not None:
+        _run([CXX, "-shared", _obj(MODULE_SOURCE), LIB, *libs, "-Wl,-rpath,$ORIGIN", "-o", MODULE + ".tmp"])
+        os.replace(MODULE + ".tmp", MODULE)
     return LIB
 
 
