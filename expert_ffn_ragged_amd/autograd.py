@@ -188,7 +188,8 @@ class DispatchRows(torch.autograd.Function):
 
 
 class CombineRows(torch.autograd.Function):
-    """out[t] = sum_i weights[t, i] * y[slots[t, i]].  Rows of dy that no slot names are +0."""
+    """out[t] = sum_i weights[t, i] * y[slots[t, i]] (weights None: a plain sum).  Rows of dy that no slot names
+    are +0."""
 
     @staticmethod
     def forward(ctx, y, slots, weights):
@@ -199,6 +200,8 @@ class CombineRows(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         y, slots, weights = ctx.saved_tensors
+        if weights is None:
+            return rd.dispatch_rows(dout.contiguous(), slots, out=torch.zeros_like(y)), None, None
         dy, dw = rd.combine_rows_bwd(dout.contiguous(), y, slots, weights, dy=torch.zeros_like(y))
         return dy, None, dw
 
@@ -247,8 +250,8 @@ def dispatch_rows(x, slots):
     return DispatchRows.apply(x, slots)
 
 
-def combine_rows(y, slots, weights):
-    """Differentiable rd.combine_rows (gradients for y and weights)."""
+def combine_rows(y, slots, weights=None):
+    """Differentiable rd.combine_rows (gradients for y and weights; weights None: a plain sum)."""
     return CombineRows.apply(y, slots, weights)
 
 
