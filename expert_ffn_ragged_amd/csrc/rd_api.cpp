@@ -346,8 +346,8 @@ int check_rows(int64_t tokens, int32_t top_k, int64_t hidden, int64_t rows) {
   if (tokens < 0 || top_k < 1 || hidden <= 0 || rows < 0) return RD_EINVAL;
   if (top_k > RD_MAX_TOP_K || hidden % 8 != 0 || hidden >= (int64_t(1) << 30) || rows >= (int64_t(1) << 31))
     return RD_EUNSUPPORTED;
-  if (tokens * top_k >= (int64_t(1) << 31) || tokens >= (int64_t(1) << 31) / ((hidden + 511) / 512))
-    return RD_EUNSUPPORTED;
+  if (tokens >= (int64_t(1) << 31) / ((hidden + 511) / 512)) return RD_EUNSUPPORTED;  // below 2^31 from here on
+  if (tokens * top_k >= (int64_t(1) << 31)) return RD_EUNSUPPORTED;
   return RD_OK;
 }
 

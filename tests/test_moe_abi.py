@@ -165,3 +165,13 @@ def test_glu_rows_leave_room_for_the_grids_stride():
     for name, ok, extra in (("rd_glu_fwd_mx8", GLU_FWD, {}), ("rd_glu_bwd_mx8", GLU_BWD, dict(slots=BIG))):
         assert _call(name, ok, rows=BIG - 1, **extra) == EUNSUPPORTED
         assert _call(name, ok, rows=BIG - (1 << 20) + 1, **extra) == EUNSUPPORTED
+
+
+@pytest.mark.parametrize("name,ok", [("rd_dispatch_rows", DISPATCH), ("rd_combine_rows", COMBINE),
+                                     ("rd_combine_rows_bwd", COMBINE_BWD)])
+def test_rows_refuses_counts_whose_products_pass_64_bits(name, ok):
+    for tokens in (1 << 40, 1 << 60, 1 << 62, (1 << 63) - 1):
+        for top_k in (1, 2, 4, 16):
+            assert _call(name, ok, tokens=tokens, top_k=top_k, hidden=8) == EUNSUPPORTED
+    assert _call(name, ok, tokens=BIG // 16, top_k=16) == EUNSUPPORTED
+    assert _call(name, ok, hidden=(1 << 63) - 8) == EUNSUPPORTED
