@@ -115,6 +115,12 @@ float real(PyObject* o) {
 }
 bool none(PyObject* o) { return o == Py_None; }
 
+// Counts that size an output are checked before it is allocated, with the library's own statuses.
+void in_range(int64_t v, int64_t most, int64_t supported) {
+  if (v < 1 || v > most) throw Status{RD_EINVAL};
+  if (v > supported) throw Status{RD_EUNSUPPORTED};
+}
+
 // One call: the GPU that its tensors live on, its stream, and the outputs it makes.
 class Call {
  public:
@@ -243,6 +249,7 @@ PyObject* route(PyObject* const* a) {
   const int32_t top_k = integer32(a[1], "top_k"), score = integer32(a[3], "score"), groups = integer32(a[4], "groups"),
                 top_groups = integer32(a[5], "top_groups"), renormalize = integer32(a[6], "renormalize");
   const float scale = real(a[7]);
+  in_range(top_k, experts, RD_MAX_TOP_K);
   const void* xp = c.at(x);
   const int32_t* limit = c.scalar(a[8], "limit");
   const float* bias = none(a[2]) ? nullptr : as<float>(c.at(given(a[2], "bias", at::kFloat, {experts})));
@@ -283,6 +290,7 @@ PyObject* group_rows(PyObject* const* a) {
   Call c(a[3]);
   const Tensor& ids = need(a[0], "ids", at::kInt);
   const int32_t experts = integer32(a[1], "experts");
+  in_range(experts, INT32_MAX, RD_MAX_GROUPS);
   const int64_t n = ids.numel(), bytes = static_cast<int64_t>(rd_group_rows_workspace_size(n, experts));
   Tensor workspace;
   if (!none(a[2]))

@@ -312,3 +312,18 @@ def test_group_rows_around_the_ids_a_lane_carries(n):
         assert np.array_equal(slots.cpu().numpy(), np.where(cls < experts, place, -1))
         assert np.array_equal(sizes.cpu().numpy(), np.bincount(cls, minlength=experts + 1)[:experts])
         assert int(total) == int((cls < experts).sum())
+
+
+def test_counts_are_refused_before_outputs_are_allocated():
+    x, ids = torch.zeros((1 << 16, 8), device=DEV), torch.zeros(64, dtype=torch.int32, device=DEV)
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for top_k in (-1, -2**31, 0, 9, 2**31 - 1):
+        with pytest.raises(rd.RDError):
+            rd.route(x, top_k)
+    for experts in (-1, -2**31, 0, 1025, 2**31 - 1):
+        with pytest.raises(rd.RDError):
+            rd.group_rows(ids, experts)
+    with pytest.raises(rd.RDError):
+        rd.route(torch.zeros((4, 64), device=DEV), 17)
+    assert torch.cuda.max_memory_allocated() < before + (1 << 16)
