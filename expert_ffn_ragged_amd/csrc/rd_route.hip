@@ -395,6 +395,10 @@ struct RouteBwdArgs {
 // d_logits of one row.  With q the chosen scores: softmax without renormalisation
 // p_i (d_i - <d, p>) for every expert; sigmoid q (1 - q) d for the chosen;
 // renormalised, with w = q / sum: w (d - <d, w>), times (1 - q) for sigmoid.
+// Where one p is near 1, its d_i - <d, p> is a small difference of nearly equal
+// numbers: the exponentials are float32, their sum and all that follows is
+// float64, so the p of a row add up to 1 within 2^-50 and the difference keeps
+// the exponentials' accuracy (in float32 a p of 1 - 3e-4 left 2e-4 of it).
 // The lanes that share a row hold it in registers, so logits are read once:
 // 8192 x 64 bf16 3.8 us, of which launching takes over half.
 template <int EPL, int LPR, bool BF16>
@@ -403,7 +407,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs p) {
   const int lane = threadIdx.x & 63, sub = lane & (LPR - 1), wave = threadIdx.x >> 6;
   const int row = p.first + blockIdx.x * (NW * RPW) + wave * RPW + lane / LPR;
   const bool in = row < p.T;
-  const long long base = static_cast<long long>(in ? row : 0) * p.E;
+  const long long at = static_cast<long long>(in ? row : 0) * p.E;
   int id = -1;
   float d = 0.f, xi = -INFINITY;
   if (in && sub < p.K) {
@@ -413,38 +417,39 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs p) {
   const bool chosen = id >= 0;
   if (chosen) {
     d = p.d_weights[static_cast<long long>(row) * p.K + sub] * p.scale;
-    xi = logit<BF16>(p.logits, base + id);
+    xi = logit<BF16>(p.logits, at + id);
   }
   const uint64_t row_bits = (LPR == 64 ? ~0ull : ((1ull << (LPR & 63)) - 1)) << (lane & ~(LPR - 1));
   const bool live = (__ballot(chosen) & row_bits) != 0;  // a row without a choice has a zero gradient
   float grad[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) grad[j] = 0.f;
-  float v = 0.f;  // the chosen expert's own term
+  double v = 0.0, base = 0.0;  // the chosen expert's own term, and its share of what all experts of the row get
   if (!p.sigmoid && !p.renorm) {
     float x[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       const int e = j * LPR + sub;
-      x[j] = live && e < p.E ? logit<BF16>(p.logits, base + e) : -INFINITY;
+      x[j] = live && e < p.E ? logit<BF16>(p.logits, at + e) : -INFINITY;
     }
     float m = x[0];
 #pragma unroll
     for (int j = 1; j < EPL; ++j) m = fmaxf(m, x[j]);
     m = row_all<LPR>(m, Max<float>());
-    float sum = 0.f;
+    double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       grad[j] = live && j * LPR + sub < p.E ? expf(x[j] - m) : 0.f;
       sum += grad[j];
     }
-    sum = row_all<LPR>(sum, Add<float>());
-    const float r = live ? 1.f / sum : 0.f;
-    const float pk = chosen ? expf(xi - m) * r : 0.f;
-    const float dot = row_all<LPR>(chosen ? d * pk : 0.f, Add<float>());
+    sum = row_all<LPR>(sum, Add<double>());
+    const double r = live ? 1.0 / sum : 0.0;
+    const double pk = chosen ? expf(xi - m) * r : 0.0;
+    const double dot = row_all<LPR>(chosen ? d * pk : 0.0, Add<double>());
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) grad[j] = live ? grad[j] * (-dot * r) : 0.f;
-    v = chosen ? pk * d : 0.f;  // joined below: p (d - dot)
+    for (int j = 0; j < EPL; ++j) grad[j] = live ? grad[j] * static_cast<float>(-dot * r) : 0.f;
+    v = pk * d;  // joined below: p (d - dot)
+    base = -pk * dot;
   } else {
     const float q = chosen ? 1.f / (1.f + expf(-xi)) : 0.f, not_q = chosen ? 1.f / (1.f + expf(xi)) : 0.f;
     if (p.renorm) {
@@ -458,21 +463,27 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs p) {
           u = xi <= 0.f ? expf(xi - m) * not_q : q;
         }
       }
-      const float sum = row_all<LPR>(u, Add<float>());
-      const float w = chosen ? u / sum : 0.f;
-      const float dot = row_all<LPR>(chosen ? d * w : 0.f, Add<float>());
-      v = chosen ? w * (d - dot) * (p.sigmoid ? not_q : 1.f) : 0.f;
+      const double sum = row_all<LPR>(static_cast<double>(u), Add<double>());
+      const double w = chosen ? u / sum : 0.0;
+      const double dot = row_all<LPR>(chosen ? d * w : 0.0, Add<double>());
+      v = chosen ? w * (d - dot) * (p.sigmoid ? not_q : 1.f) : 0.0;
     } else {
       v = chosen ? d * q * not_q : 0.f;
     }
   }
+  // the chosen experts' gradients take the place of their share; an expert that is named twice adds up
   const int first = lane & ~(LPR - 1);
   for (int i = 0; i < p.K; ++i) {
+    const double other = __shfl(v, first + i, 64);
+    base += __shfl(id, first + i, 64) == id ? other : 0.0;
+  }
+  const float own = static_cast<float>(base);
+  for (int i = 0; i < p.K; ++i) {
     const int e = __shfl(id, first + i, 64);
-    const float t = __shfl(v, first + i, 64);
+    const float t = __shfl(own, first + i, 64);
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
-      if (e == j * LPR + sub) grad[j] += t;
+      if (e == j * LPR + sub) grad[j] = t;
   }
   if (!in) return;
 #pragma unroll
@@ -480,9 +491,9 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs p) {
     const int e = j * LPR + sub;
     if (e < p.E) {
       if constexpr (BF16)
-        static_cast<uint16_t*>(p.d_logits)[base + e] = static_cast<uint16_t>(f32_to_bf16(grad[j]));
+        static_cast<uint16_t*>(p.d_logits)[at + e] = static_cast<uint16_t>(f32_to_bf16(grad[j]));
       else
-        static_cast<float*>(p.d_logits)[base + e] = grad[j];
+        static_cast<float*>(p.d_logits)[at + e] = grad[j];
     }
   }
 }

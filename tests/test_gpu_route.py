@@ -327,3 +327,36 @@ def test_counts_are_refused_before_outputs_are_allocated():
     with pytest.raises(rd.RDError):
         rd.route(torch.zeros((4, 64), device=DEV), 17)
     assert torch.cuda.max_memory_allocated() < before + (1 << 16)
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+@pytest.mark.parametrize("experts,top_k", [(64, 1), (128, 2), (300, 4)])
+def test_gradient_of_a_router_that_is_almost_sure(experts, top_k, score, renorm):
+    """One expert far above the others: its gradient is the small difference of two nearly equal terms,
+    p_i (d_i - sum d p) = p_i (d_i (1 - p_i) - sum of the others' d p), and keeps its relative accuracy.  Each factor
+    is a quotient of float32 exponentials, off by rel (see above), three in a product, and a rounding each."""
+    say(f"route_bwd almost sure {experts} {top_k} {score} {renorm}")
+    tokens = 40
+    x = logits_of(tokens, experts, torch.float32, 5 * experts, std=1.0)
+    x = x - (14.0 if score == "sigmoid" else 0.0)
+    x[torch.arange(tokens), torch.arange(tokens) * 7 % experts] += torch.linspace(4.0, 16.0, tokens)
+    d = torch.randn((tokens, top_k), generator=torch.Generator().manual_seed(3))
+    xd = x.to(DEV)
+    _, ids = rd.route(xd, top_k, score=score, renormalize=renorm)
+    got = rd.route_bwd(xd, ids, d.to(DEV), score=score, renormalize=renorm).cpu().double().numpy()
+    xv, dv, ids = x.double().numpy(), d.double().numpy(), ids.cpu().numpy()
+    want = moe.route_bwd(xv, ids, dv, score, renorm)
+    rel = rel_error(xv, experts)
+    for t in range(tokens):
+        xt, c = xv[t].astype(np.longdouble), ids[t]
+        p = np.exp(xt - xt.max()) if score == "softmax" else 1 / (1 + np.exp(-xt))
+        p = p / (p[c].sum() if renorm else p.sum())
+        mags = np.zeros(experts)
+        if not renorm:
+            mags += p * (np.abs(dv[t]) * p[c]).sum()
+        for i, e in enumerate(c):
+            others = sum(abs(dv[t, j]) * p[c[j]] for j in range(top_k) if j != i)
+            rest = p[c].sum() - p[e] if renorm else p.sum() - p[e]
+            mags[e] = p[e] * (abs(dv[t, i]) * rest + others) * (1 if score == "softmax" else 1 / (1 + np.exp(xt[e])))
+        tol = (3 * rel + 4 * 2.0 ** -23) * mags
+        assert np.all(np.abs(got[t] - want[t]) <= tol), (t, np.max(np.abs(got[t] - want[t]) - tol))
