@@ -51,7 +51,8 @@ def parse():
                     help="only the headline step (for profiler runs), no extra workloads")
     ap.add_argument("--sweep", action="store_true",
                     help="time every tile shape of every grouped GEMM on the workloads and print the table")
-    ap.add_argument("--profile", choices=("backward", "upproj", "decode", "packed", "routed_train", "routed_decode"),
+    ap.add_argument("--profile", choices=("backward", "upproj", "decode", "packed", "routed_train", "routed_decode",
+                                              "mx_rows"),
                     help="only run one workload's kernels, --warmup + --steps times each, for a profiler")
     ap.add_argument("--settle", type=int, default=0,
                     help="with --profile: untimed passes before the warmup, flushed with --cold (the headline "
@@ -818,6 +819,25 @@ def routed_decode(d=4096, h=768):
     return step
 
 
+def mx_rows(experts=64, k=4096, n=2048):
+    """Products of 8192 rows over Zipf-sized experts with 4-bit weights: [4-bit rows, 8-bit rows]."""
+    import torch
+
+    from expert_ffn_ragged_amd import rd, workloads
+
+    gs = torch.from_numpy(workloads.group_sizes(2)).to("cuda")
+    rows = int(gs.sum())
+    x = workloads.bf16_normal((rows, k), 1.0, 9011, "cuda")
+    w = rd.quantize_mx(workloads.bf16_normal((experts, n, k), 0.02, 9012, "cuda"))
+    out = torch.empty((rows, n), dtype=torch.bfloat16, device="cuda")
+
+    def product(bits):
+        q = rd.quantize_mx(x, bits=bits)
+        return lambda: rd.ragged_dot_mx(*q, *w, gs, out=out)
+
+    return [product(4), product(8)]
+
+
 def profile_run(which, steps, warmup, cold=False, settle_steps=0):
     """One workload's kernels and nothing else (no timing, no oracle), for rocprofv3 runs; with cold, the
     caches are flushed before every pass as in the headline's timing; settle_steps untimed passes (flushed
@@ -855,6 +875,8 @@ def profile_run(which, steps, warmup, cold=False, settle_steps=0):
         ops = [lambda: rd.ragged_dot(d["x"], d["w"], d["gs"], out=o, workspace=ws)]
     elif which.startswith("routed"):
         ops = [routed_train() if which == "routed_train" else routed_decode()]
+    elif which == "mx_rows":
+        ops = mx_rows()
     else:  # the packed expert buffer at limit 126156: the window+limit forward, GLU fwd / bwd, unsort backward
         d = workloads.make(4, "cuda", parts=("x", "w", "fused", "d_out", "ug", "uy", "uw"))
         lim = torch.tensor([d["limit"]], dtype=torch.int32, device="cuda")

@@ -54,6 +54,8 @@ constexpr int kChunks = 8;  // 16-byte chunks of a row that a lane of dispatch c
 // what bounds the copy is the writing, which goes on in whole rows: the packed buffer's 126152 rows of 8 KB take
 // 221 us (5.3 TB/s with x's bytes), where one wave that wrote the row to all of its slots in turn took 235, sorted
 // rows that were gathered 289, and 4 KB a wave 227.  (1 KB a wave gains 0.2 us below 128 choices and loses from 512.)
+// Rows of 1024 and more reach 6.3 TB/s where they fit the caches, 512 4.4, 256 2.4, 128 1.2: a wave a row, and most of
+// its loads empty.
 __global__ __launch_bounds__(kThreads) void dispatch_rows_kernel(RowsArgs p) {
   const int lane = threadIdx.x & 63;
   const long long unit = wave_index(p);
@@ -75,7 +77,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_rows_kernel(RowsArgs p) {
 }
 
 // One wave per (token, part of its row): the K rows' parts are read four at a time and added in the order
-// of the choices.  Bandwidth-bound: 8192 tokens of 4 rows of 4096, 0.34 GB, 58 us (5.8 TB/s).
+// of the choices.  Bandwidth-bound: 8192 tokens of 4 rows of 4096, 0.34 GB, 58 us (5.8 TB/s); rows of 512 5.3 TB/s,
+// 256 3.9, 128 2.3.
 __global__ __launch_bounds__(kThreads) void combine_rows_kernel(RowsArgs p) {
   constexpr int AT = 4;
   const int lane = threadIdx.x & 63;
@@ -116,7 +119,8 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(RowsArgs p) {
 
 // One wave per choice: dy[slot] = w g[t], dw = <g[t], y[slot]>, the products exact in float32 and added
 // in float64 in a fixed order, so dw is the exact dot rounded once.  Bandwidth-bound: 8192 tokens of 4 rows of 4096,
-// 0.60 GB (g's rows come from the caches after the first choice), 112 us (5.4 TB/s).
+// 0.60 GB (g's rows come from the caches after the first choice), 112 us (5.4 TB/s); rows of 512 5.5 TB/s, 256 3.6,
+// 128 1.9.
 __global__ __launch_bounds__(kThreads) void combine_rows_bwd_kernel(RowsArgs p) {
   const int lane = threadIdx.x & 63;
   const long long unit = wave_index(p);

@@ -172,10 +172,11 @@ __device__ __forceinline__ i32x8_t operand(const i32x4_t (&v)[2]) {
 // with no barrier but the two of a pass's sums.
 //
 // The limits are the largest mean of rows a local group and the most tiles where
-// this was faster: with 16 rows of 4-bit x and 4096 x 2048 weights, one group (16 tiles)
-// took 6.9 us against 12.1 in tiles, 4 groups (64) 9.5 against 12.0, 8 groups
-// (128) 12.6 against 12.8, and 16 groups of 4096 x 1536 (192) 14.5 against 13.1;
-// 1536 rows over 128 groups of these took 98 us against 60.
+// this was faster: with 16 rows of 4-bit x and 4096 x 2048 weights, one group (16
+// tiles) took 7.0 us against 11.9 in tiles (8-bit x 8.0 against 14.3), 4 groups (64)
+// 8.6 against 12.2 (10.4, 14.7), 8 groups (128) 12.5 against 13.0 (14.5, 15.1), and
+// 16 groups of 4096 x 1536 (192) 14.6 against 13.4 (17.5, 15.3); 1536 rows over 128
+// groups of these took 98 us against 60.
 constexpr int kFewRows = 24, kFewTiles = 128;
 constexpr int kWin = 512, kFewN = 2;
 

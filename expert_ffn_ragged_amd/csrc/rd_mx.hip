@@ -147,8 +147,8 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx_kernel(const uint8_t* 
 }
 
 // act = silu(gate) * up of the bf16 input, and that input in MX 8-bit elements; one wave per row, so that a limit
-// cuts whole waves and the 8-bit copy costs no second reading.  Bandwidth-bound: 32768 rows of h 1024, 0.27 GB, 44
-// us (6.2 TB/s).
+// cuts whole waves and the 8-bit copy costs no second reading.  Bandwidth-bound: 32768 rows of h 1024, 0.27 GB, 43
+// us (6.3 TB/s), and so down to h 512, where every lane has a chunk; h 256 reaches 4.7 TB/s, 128 2.6, 64 1.4.
 __global__ __launch_bounds__(kThreads) void glu_fwd_mx8_kernel(const uint16_t* __restrict__ fused,
                                                                const int32_t* __restrict__ limp,
                                                                uint16_t* __restrict__ act, uint8_t* __restrict__ codes,
@@ -191,7 +191,8 @@ struct GluBwdArgs {
 
 // One wave per row r with slot s and weight w: act = w silu(g) u, d_fused = w d times the GLU's partial
 // derivatives, dot[s] = <d, silu(g) u>, which one wave sums: no partial sums, and the same result every time.
-// Bandwidth-bound: 32768 rows of h 1024, 0.34 GB, 64 us (5.3 TB/s).
+// Bandwidth-bound: 32768 rows of h 1024, 0.34 GB, 60 us (5.7 TB/s), h 512 5.6 TB/s; narrower rows leave lanes without
+// a chunk: h 256 3.4 TB/s, 128 1.9, 64 1.1.
 __global__ __launch_bounds__(kThreads) void glu_bwd_mx8_kernel(GluBwdArgs p) {
   const int L = static_cast<int>(clamp_limit(p.limp, p.rows));
   const int hc = p.h >> 3, lane = threadIdx.x & 63;
@@ -234,7 +235,8 @@ template <int BITS, class T>
 void quantize_as(const T* x, const int32_t* limit, uint8_t* codes, uint8_t* scales, long long rows, long long cols,
                  hipStream_t stream) {
   // one chunk a lane, four times the waves: 512 x 4096 to 8 bits 3.1 us against 4.6, 8192 x 4096 19.4 against 21.2,
-  // 32768 x 2048 34.6 against 38.0; 65536 x 4096 to 4 bits and back 234 against 225
+  // 32768 x 2048 34.6 against 38.0; 65536 x 4096 to 4 bits and back 234 against 225.  Float32, to 4 bits and back:
+  // 2^24 elements 38.6 against 39.4, 2^25 81 against 80, 2^27 355 against 349, 2^28 766 against 745
   if (rows * cols <= kOneChunk)
     quantize_mx_kernel<BITS, 1>
         <<<stream_grid(rows * (cols / 8), 32), kThreads, 0, stream>>>(x, limit, codes, scales, rows, cols);
