@@ -338,9 +338,10 @@ __global__ __launch_bounds__(kThreads, 2) void ragged_dot_mx_few(MxArgs p) {
 // workgroups a CU, each of which fills the gaps that the other's barriers,
 // first loads and stores leave.  Both operands of a window lie in a ring of LDS
 // stages; all but the one being multiplied are on their way.  A tile with more
-// than 64 rows gives each wave 64 x 64 outputs and is bound by the loads into
-// its CU (8192 rows of one group, 2048 x 4096, 4-bit x: 55 us, 2.5 PFLOP/s).  One with
-// fewer gives it all rows and 32 columns, its stages are smaller and there are
+// than 64 rows gives each wave 64 x 64 outputs (8-bit x: 32 x 128) and is bound by the
+// loads into its CU (8192 rows of one group, 2048 x 4096, 4-bit x: 55 us, 2.5 PFLOP/s).
+// One with fewer gives it all rows and 32 columns (8-bit x: 16 rows and more
+// columns), its stages are smaller and there are
 // more of them, so that a tile of a small group is a stream of its weights:
 // decode takes 60 us for 300 MB, 5.0 TB/s.
 constexpr int kTileM = 128, kTileN = 128, kTileThreads = 256, kTileWaves = 4;
@@ -522,12 +523,14 @@ __device__ __forceinline__ void mx_tile(const MxArgs& p, const TileAt& t, char* 
 // starting the workgroups at different windows, to spread rows of a power-of-two
 // stride over the channels, cost up to 25 %.
 //
-// What bounds it now are the loads into the CUs, whose L2 misses and hits add up:
-// the up-projection (8192 rows over 64 Zipf groups of 2048 x 4096, 4-bit x) loads 285 MB
-// of weights at 5 TB/s and 370 MB more from the L2s at 9.3, 97 us of the 98
-// measured.  Other orders of the tiles do not change that: groups with the most
-// rows first, large tiles before small ones, or one of each on every CU gained
-// nothing there and lost where groups are of one size.
+// What bounds it now is what is read past the L2s: the up-projection (8192 rows
+// over 64 Zipf groups of 2048 x 4096) with 4-bit x reads 501 MB there, of which the
+// weights are 285 and x comes once for every XCD that has a strip, in 96 us (5.2
+// TB/s), and as much again from the L2s; with 8-bit x 790 MB in 173 us, where
+// the second instruction and the split add to the loads, since a stage or two is
+// all that is on its way.  Other orders of the tiles do not change that: groups
+// with the most rows first, large tiles before small ones, or one of each on
+// every CU gained nothing there and lost where groups are of one size.
 template <int XB, int MAXL>
 __global__ __launch_bounds__(kTileThreads, kTileWgs<MAXL>) void ragged_dot_mx_tile(MxArgs p) {
   constexpr int RING = kRingBytes<MAXL>;

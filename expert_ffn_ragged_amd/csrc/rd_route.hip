@@ -507,8 +507,9 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs p) {
 // slot's place is the number of slots before it: results do not depend on
 // timing.  Up to 4096 ids are one workgroup and one launch; more take a first
 // launch that counts each workgroup's classes, and many more a second that adds
-// the counts up.  Latency sets the time, not the
-// bytes: 512 ids of 256 experts 3.3 us, 225280 ids (2.7 MB) 11.9.
+// the counts up.  Latency sets the time of few ids, not the bytes: 512 ids of 256
+// experts 3.3 us, 225280 ids (2.7 MB) 11.9.  4194304 ids (50 MB) take 44: they are
+// read and classified twice, and the counts' reads lie a class apart.
 constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64, kSortMaxR = 8;
 constexpr int kSortClasses = (RD_MAX_GROUPS + kSortThreads) / kSortThreads;  // classes a thread carries at most
 static_assert(kSortClasses * kSortThreads >= RD_MAX_GROUPS + 1, "every class has a thread");
